@@ -121,7 +121,8 @@ struct CausalNode : torch::autograd::Function<CausalNode> {
         const Causal s(x, w, bias, state, in[4], ctx->saved_data["act"].toInt());
         const auto sums = x.options().dtype(at::kFloat);
         const Tensor dx = at::empty({s.B, s.T, s.C}, x.options()), dw = at::empty({s.W, s.C}, sums), db = like(bias);
-        const Tensor ds = state.defined() && ctx->needs_input_grad(3) ? like(state) : Tensor();
+        // the node has edges for the tensors that are there: x, w, the bias, the state
+        const Tensor ds = state.defined() && ctx->needs_input_grad(2 + bias.defined()) ? like(state) : Tensor();
         const size_t size = dwconv_causal_bwd_workspace_size(s.B, s.T, s.C, s.W, s.dt);
         const Tensor work = bytes(size, x);
         check(dwconv_causal_bwd(s.B, s.T, s.C, s.W, s.dt, address(dy), dy.stride(0), dy.stride(1), address(x),
