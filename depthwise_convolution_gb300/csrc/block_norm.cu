@@ -566,6 +566,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 128 ? (NV * VEC <= 8 ? 4 : 3) : 
         float mean = 0.f, rstd = 1.f;
         if (a.w_post) {
             row_stats<NV, VEC>(hat, cols, a, group, mean, rstd);
+            if (!live) rstd = 0.f;  // zeros stand in for a missing row: nothing for the column sums, whatever eps
             normalise<NV, VEC>(hat, a, mean, rstd);
         }
 #pragma unroll
@@ -600,6 +601,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 128 ? (NV * VEC <= 8 ? 4 : 3) : 
             }
             float hm, hr;
             row_stats<NV, VEC>(x, cols, a, group, hm, hr);
+            if (!live) hr = 0.f;
             normalise<NV, VEC>(x, a, hm, hr);
 #pragma unroll
             for (int q = 0; q < NV; ++q) {

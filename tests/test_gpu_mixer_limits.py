@@ -1,0 +1,34 @@
+"""The token mixer at the edges of what it accepts: widths, gates and values where a kernel's form changes or a sum could
+leave the finite numbers.  Tolerances are those of the operator's own test file, which derives them."""
+import pytest
+import torch
+
+import depthwise_convolution_gb300 as dw
+import mixer_reference as ref
+import test_gpu_block_norm as norms
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("dtype,shape,parts", [
+    ("fp32", (7, 48), "rgpsn"), ("fp32", (5, 5), "rpsn"), ("bf16", (4999, 136), "rgpsn"), ("fp16", (3, 100), "gp"),
+    ("fp32", (3001, 96), "gpsn"), ("bf16", (5001, 97), "rpsn"), ("fp16", (2049, 1024), "rpsn"),
+])
+def test_norm_gradients_without_an_epsilon(dtype, shape, parts, kind):
+    """CTAs that hold more rows than there are: what stands in for the missing ones adds nothing to the column sums."""
+    args, dh, dn = norms.inputs(dtype, shape, parts, seed=2)
+    got = dw.dwconv_block_norm_bwd(dh, dn, *args, kind=kind, gate_act="silu", eps=0.0)
+    leaves = [ref.leaf(a) for a in args]
+    outs = ref.block_norm(*leaves, kind, "silu", 0.0)
+    pairs = [(o, ref.wide(d)) for o, d in zip(outs, (dh, dn)) if o is not None and d is not None]
+    want = iter(torch.autograd.grad([o for o, _ in pairs], [x for x in leaves if x is not None], [d for _, d in pairs]))
+    want = [None if x is None else next(want) for x in leaves]
+    size = sum(d.abs().amax(-1, keepdim=True) for _, d in pairs) * (1 + max(
+        a.abs().max().item() for a in args if a is not None))
+    for name, a, r in zip(("dy", "dresidual", "dgate"), got[:3], want[:3]):
+        if a is not None:
+            ref.assert_near(a, r, name, dtype, 2e-5, r.abs().amax(-1, keepdim=True) + 0.1 * size)
+    for name, a, r in zip(("dw_post", "dscale", "dw_pre"), got[3:], want[3:]):
+        if a is not None:
+            ref.assert_near(a, r, name, "fp32", 1e-5, torch.full_like(r, shape[0] ** 0.5 * size.max().item()))
