@@ -117,14 +117,15 @@ template <typename F> __device__ __forceinline__ void with_act(int act, F &&f) {
     else f(std::integral_constant<int, DWCONV_GATE_NONE>{});
 }
 
-// A thread's columns of a row of any tensor, and of the weight vectors.
+// A thread's columns of a row of any tensor, and of the weight vectors; the row's
+// end where a vector of its lies beyond.
 template <int VEC, int NV> struct Cols {
     int c[NV];
     bool in[NV];
     __device__ __forceinline__ Cols(const NormArgs &a, int g) {
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
-            c[q] = (q * a.G + g) * VEC;
+            c[q] = min((q * a.G + g) * VEC, a.C);
             in[q] = c[q] < a.C;
         }
     }
@@ -193,11 +194,12 @@ template <int VEC, int NV, bool HOLD> struct Weight {
 
 // The same out of shared memory, where the backward pass, which has no
 // registers left for them, keeps its weight vectors: ones where a vector is
-// absent, zeros beyond the row.
+// absent, and behind the row one vector of zeros for all columns beyond it.
 template <int VEC, int NV> struct SharedWeight {
     const float *w;
+    static __host__ __device__ int size(int C) { return C + VEC; }
     __device__ __forceinline__ SharedWeight(const NormArgs &a, const float *from, float *to) : w(to) {
-        for (int c = threadIdx.x; c < a.G * NV * VEC; c += blockDim.x) to[c] = c < a.C ? (from ? from[c] : 1.f) : 0.f;
+        for (int c = threadIdx.x; c < size(a.C); c += blockDim.x) to[c] = c < a.C ? (from ? from[c] : 1.f) : 0.f;
     }
     __device__ __forceinline__ Pack<float, VEC> at(const Cols<VEC, NV> &cols, int q) const {
         if constexpr (VEC == 1) {
@@ -530,7 +532,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 128 ? (NV * VEC <= 8 ? 4 : 3) : 
     __shared__ RowRing ring;
     extern __shared__ __align__(128) unsigned char smem[];  // weights, then the ring; afterwards [rows per CTA][C] column sums
     float *shared_cols = reinterpret_cast<float *>(smem), *weights = shared_cols;
-    const int width = a.G * NV * VEC;
+    const int width = SharedWeight<VEC, NV>::size(a.C);
     unsigned char *stages = smem + 3 * width * sizeof(float);
     after_previous();
     Group group(red, a.G);
@@ -771,7 +773,7 @@ cudaError_t fwd_run(const NormArgs &a, int threads, cudaStream_t st) {
 template <typename T, int VEC, int NV, int MAXT, bool RING>
 cudaError_t bwd_run(const NormArgs &a, int threads, float *dwp, float *dsc, float *dwr, cudaStream_t st) {
     const int per = threads / a.G;
-    const size_t smem = std::max(3 * sizeof(float) * a.G * NV * VEC + (RING ? a.stages * round_bytes<T>(a, per) : 0),
+    const size_t smem = std::max(3 * sizeof(float) * SharedWeight<VEC, NV>::size(a.C) + (RING ? a.stages * round_bytes<T>(a, per) : 0),
                                  per > 1 ? (size_t)per * a.C * sizeof(float) : 0);
     auto kern = block_norm_bwd_kernel<T, VEC, NV, MAXT, RING>;
     long long grid = 0;
@@ -792,7 +794,8 @@ cudaError_t bwd_run(const NormArgs &a, int threads, float *dwp, float *dsc, floa
 // are at most 512 threads an SM and a call is a chain of latencies: 7 rows of 768
 // in fp32 take 5.2 us instead of 15.4, 152 rows of 4096 in bf16 9.3 instead of
 // 10.4, and 304 rows of 4096, beyond the rule, would take 12.4 instead of 11.4.
-// MOST, without a ring, for the widest rows.
+// MOST, without a ring, for the widest rows and those whose ring has no room
+// beside `fixed` bytes.
 template <typename T, int VEC, int FEW, typename F> cudaError_t with_shape(NormArgs &a, size_t fixed, F &&f) {
     constexpr bool RING = VEC > 1;
     constexpr int MOST = kMaxNormWidth / 512 / VEC;
@@ -803,7 +806,7 @@ template <typename T, int VEC, int FEW, typename F> cudaError_t with_shape(NormA
         const size_t round = round_bytes<T>(a, std::max(threads, a.G) / a.G);
         // three rounds while that leaves room for four CTAs an SM
         a.stages = 3 * round <= 56 * 1024 ? 3 : 2;
-        return !RING || a.stages * round + fixed <= 220 * 1024;
+        return !RING || a.stages * round + fixed <= 224 * 1024;
     };
     using std::integral_constant;
     using Ring = std::bool_constant<RING>;
@@ -823,7 +826,7 @@ template <typename T, int VEC> cudaError_t fwd_launch(NormArgs a, cudaStream_t s
 
 template <typename T, int VEC>
 cudaError_t bwd_launch(NormArgs a, float *dwp, float *dsc, float *dwr, cudaStream_t st) {
-    return with_shape<T, VEC, (VEC == 1 ? 8 : 2)>(a, 3 * sizeof(float) * a.C, [&](auto nv, auto most, auto ring, int threads) {
+    return with_shape<T, VEC, (VEC == 1 ? 8 : 2)>(a, 3 * sizeof(float) * (a.C + VEC), [&](auto nv, auto most, auto ring, int threads) {
         return bwd_run<T, VEC, decltype(nv)::value, decltype(most)::value, decltype(ring)::value>(a, threads, dwp, dsc, dwr,
                                                                                                  st);
     });

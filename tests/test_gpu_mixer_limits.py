@@ -10,6 +10,13 @@ import test_gpu_block_norm as norms
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("C", [6672, 6680, 6912, 7040, 7048])
+def test_norm_gradients_where_rows_stop_fitting_shared_memory(dtype, C):
+    for rows in (3, 400):
+        norms.test_gradients(dtype, (rows, C), "rms", "silu", "rgpsn", "both")
+
+
 @pytest.mark.parametrize("kind", ["rms", "layer"])
 @pytest.mark.parametrize("dtype,shape,parts", [
     ("fp32", (7, 48), "rgpsn"), ("fp32", (5, 5), "rpsn"), ("bf16", (4999, 136), "rgpsn"), ("fp16", (3, 100), "gp"),
