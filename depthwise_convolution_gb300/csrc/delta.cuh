@@ -14,6 +14,11 @@ namespace dwc {
 constexpr float kDeltaEps = 1e-6f;
 constexpr int kDeltaMaxK = 256;       // recurrent kernel
 constexpr int kDeltaChunk = 64;       // tokens of a chunk
+// Log decays below this reset the state just as well (e^g is zero in fp32 from
+// -104 on), and sums of them leave what stands beside them in the sum intact:
+// 64 of them as hi + lo floats are good to 2^-28.  Minus infinity would not be
+// (its differences are not numbers), nor the lowest float (it swallows the rest).
+constexpr float kDeltaReset = -1e4f;
 
 struct DeltaArgs {
     int B, T, Hk, Hv, K, V;

@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 1 : 4) delta_pr
         float be[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            s[j] = g_bits[j].get<T>(a.gate_f32);
+            const float g = g_bits[j].get<T>(a.gate_f32);
+            s[j] = g < kDeltaReset ? kDeltaReset : g;
             be[j] = b_bits[j].get<T>(a.gate_f32);
         }
         double run = s[0] + s[1];

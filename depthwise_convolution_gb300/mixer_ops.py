@@ -446,8 +446,8 @@ def _saved(saved, dev, shape):
 
 def dwconv_delta_fwd(q, k, v, g, beta, scale=None, qk_norm=False, state=None, lengths=None, return_state=False,
                      out=None, state_out=None, saved=None, workspace=None, stream=None):
-    """Gated delta rule over sequences: q, k [B,T,Hk,K], v [B,T,Hv,V], g (log decay) and
-    beta [B,T,Hv] of q's dtype or float32; scale defaults to K**-0.5; qk_norm divides q and
+    """Gated delta rule over sequences: q, k [B,T,Hk,K], v [B,T,Hv,V], g (log decay; minus
+    infinity resets the state) and beta [B,T,Hv] of q's dtype or float32; scale defaults to K**-0.5; qk_norm divides q and
     k by their norms.  state [B,Hv,K,V] float32 (None: zeros), lengths [B] int32.  Returns
     o [B,T,Hv,V], with return_state (o, state_out).  saved: a buffer of
     dwconv_delta_saved_size bytes that dwconv_delta_bwd can then take over."""

@@ -6,6 +6,8 @@ import torch
 import depthwise_convolution_gb300 as dw
 import mixer_reference as ref
 import test_gpu_block_norm as norms
+import test_gpu_delta as delta
+import test_gpu_delta_bwd as delta_bwd
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +41,38 @@ def test_norm_gradients_without_an_epsilon(dtype, shape, parts, kind):
     for name, a, r in zip(("dw_post", "dscale", "dw_pre"), got[3:], want[3:]):
         if a is not None:
             ref.assert_near(a, r, name, "fp32", 1e-5, torch.full_like(r, shape[0] ** 0.5 * size.max().item()))
+
+
+def resets(g, at, value):
+    g = g.clone()
+    for t in at:
+        if t < g.shape[1]:
+            g[:, t, ::2] = value
+    return g
+
+
+@pytest.mark.parametrize("value", ["-inf", "lowest"])
+@pytest.mark.parametrize("dtype,gates", [("bf16", "bf16"), ("fp16", "fp16"), ("fp16", "fp32"), ("fp32", "fp32")])
+@pytest.mark.parametrize("T", [8, 150])
+def test_gates_that_reset_a_state(T, dtype, gates, value):
+    """A log decay of minus infinity, or the lowest value of its type, forgets everything and nothing else: two in a
+    row, at both ends of a chunk, within one.  Sequences, their gradients and single tokens."""
+    gt = ref.TYPES[gates]
+    (q, k, v, g, b), state = delta.inputs(dtype, 2, T, 1, 2, 64, 32, gates=gt, seed=11)
+    g = resets(g, (0, 3, 4, 63, 64, 90, 127, 149), float("-inf") if value == "-inf" else torch.finfo(gt).min)
+    args = [q, k, v, g, b]
+    leaves = [ref.leaf(a) for a in (*args, state)]
+    ro, rs = ref.delta(*leaves[:5], None, True, leaves[5], None)
+    o, after = dw.dwconv_delta_fwd(*args, qk_norm=True, state=state, return_state=True)
+    ref.assert_close_in_norm(o, ro, "o", delta.REL[dtype])
+    ref.assert_close_in_norm(after, rs, "state", 2e-5)
+    pool = state.clone()
+    steps = torch.stack([dw.dwconv_delta_step(*(a[:, t] for a in args), pool, qk_norm=True) for t in range(T)], 1)
+    ref.assert_close_in_norm(steps, ro, "single tokens", delta.REL[dtype])
+    ref.assert_close_in_norm(pool, rs, "state after single tokens", 2e-5)
+    do = torch.randn(v.shape, generator=torch.Generator().manual_seed(12)).to(v.dtype).cuda()
+    got = dw.dwconv_delta_bwd(do, *args, qk_norm=True, state=state, need_dstate=True)
+    want = torch.autograd.grad((ro * ref.wide(do)).sum(), leaves)
+    for name, a, r in zip((*delta_bwd.NAMES, "dstate"), got, want):
+        ref.assert_close_in_norm(a, r, name, delta_bwd.REL[dtype])
+    assert not got[3][g < -1e4].any()  # nothing depends on how far below
