@@ -73,6 +73,16 @@ struct Frag {
     unsigned r[4];
 };
 
+constexpr float kNan = __builtin_nanf("");
+__device__ __forceinline__ bool is_finite(float v) { return fabsf(v) < __int_as_float(0x7F800000); }
+__device__ __forceinline__ float finite_or_zero(float v) { return is_finite(v) ? v : 0.f; }
+// The largest of three (NaN if one is NaN): one instruction.
+__device__ __forceinline__ float max_or_nan(float a, float b, float c) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+
 // 2^-e and 2^e for m in [2^e, 2^(e+1)); 1 for zero and subnormals.
 __device__ __forceinline__ void pow2_scale(float m, float &down, float &up) {
     unsigned e = __float_as_uint(m) >> 23;

@@ -53,17 +53,20 @@ template <int KS> struct TeamBuf {
 };
 
 // Largest magnitude of a row over its four lanes: rows lane / 4 (entries 0, 1)
-// and lane / 4 + 8 (2, 3) of N tiles.
-template <int N> __device__ __forceinline__ void row_max(const float (&x)[N][4], float (&m)[2]) {
+// and lane / 4 + 8 (2, 3) of N tiles.  NAN_TOO: a NaN in a row is its largest.
+template <bool NAN_TOO> __device__ __forceinline__ float largest(float a, float b, float c = 0.f) {
+    return NAN_TOO ? max_or_nan(a, b, c) : fmaxf(fmaxf(a, b), c);
+}
+template <int N, bool NAN_TOO = false> __device__ __forceinline__ void row_max(const float (&x)[N][4], float (&m)[2]) {
     m[0] = m[1] = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) m[j >> 1] = fmaxf(m[j >> 1], fabsf(x[i][j]));
+        for (int q = 0; q < 2; ++q) m[q] = largest<NAN_TOO>(m[q], fabsf(x[i][2 * q]), fabsf(x[i][2 * q + 1]));
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        m[q] = fmaxf(m[q], __shfl_xor_sync(0xFFFFFFFFu, m[q], 1));
-        m[q] = fmaxf(m[q], __shfl_xor_sync(0xFFFFFFFFu, m[q], 2));
+        m[q] = largest<NAN_TOO>(m[q], __shfl_xor_sync(0xFFFFFFFFu, m[q], 1));
+        m[q] = largest<NAN_TOO>(m[q], __shfl_xor_sync(0xFFFFFFFFu, m[q], 2));
     }
 }
 template <int N> __device__ __forceinline__ void scale_rows(float (&x)[N][4], const float (&f)[2]) {
@@ -80,12 +83,12 @@ __device__ __forceinline__ void share_rows(float (&to)[16], const float (&m)[2],
         to[lane / 4 + 8] = m[1];
     }
 }
+template <bool NAN_TOO = false>
 __device__ __forceinline__ void most_rows(const float (&from)[kTeam][16], int lane, float (&m)[2]) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        m[q] = from[0][lane / 4 + 8 * q];
-#pragma unroll
-        for (int i = 1; i < kTeam; ++i) m[q] = fmaxf(m[q], from[i][lane / 4 + 8 * q]);
+        const int r = lane / 4 + 8 * q;
+        m[q] = largest<NAN_TOO>(largest<NAN_TOO>(from[0][r], from[1][r], from[2][r]), from[3][r]);
     }
 }
 
@@ -110,6 +113,37 @@ struct Domain {
         down[q] *= f;
         unsigned e = __float_as_uint(down[q]) >> 23;
         up[q] = __uint_as_float((254 - e) << 23);
+    }
+};
+
+// Where a row (a column of the state) meets a value, key or gate that is no finite
+// number: the first token of a warp's block from which on it is lost (16: none).
+// The zeros above the diagonals of M and P would spread it to tokens before, so
+// entries from it on stay out of the products, the outputs from it on and the
+// state are lost by themselves.  M and P hold numbers whatever the inputs.
+struct Cut {
+    int at[2] = {16, 16};
+    // x: the block of l beta R; most: the largest in the blocks of all warps
+    __device__ __forceinline__ void find(const float (&x)[2][4], const float (&most)[kTeam][16], int me, int lane) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+            for (int i = 1; i >= 0; --i)
+#pragma unroll
+                for (int j = 1; j >= 0; --j)
+                    if (!is_finite(x[i][2 * q + j])) at[q] = 8 * i + 2 * (lane % 4) + j;
+            at[q] = min(at[q], __shfl_xor_sync(0xFFFFFFFFu, at[q], 1));
+            at[q] = min(at[q], __shfl_xor_sync(0xFFFFFFFFu, at[q], 2));
+            for (int i = 0; i < me; ++i)
+                if (!is_finite(most[i][lane / 4 + 8 * q])) at[q] = 0;
+        }
+    }
+    __device__ __forceinline__ void fill(float (&x)[2][4], int lane, float from_there_on) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (8 * i + 2 * (lane % 4) + (j & 1) >= at[j >> 1]) x[i][j] = from_there_on;
     }
 };
 
@@ -236,7 +270,7 @@ __device__ __forceinline__ void walk(const DeltaArgs &a, const Saved &saved, Rin
                 }
             }
             if (c + 1 < live) vt.load(v, a.v_s[1], (c + 1) * kC, n, col, a.V, lane, mine);
-            row_max<2>(B, m);
+            row_max<2, true>(B, m);
             share_rows(buf.most[me], m, lane);
             auto share_blocks = [&] {
                 float t[2][4];
@@ -252,18 +286,39 @@ __device__ __forceinline__ void walk(const DeltaArgs &a, const Saved &saved, Rin
             share_blocks();
             team_sync(team);
             // Where the scale of a column no longer suits both U and the state it moves,
-            // and the blocks are shared once more: all warps see the same columns.
+            // or what they need is no number, the blocks are shared once more: all warps
+            // see the same columns.
             const float last = vec[F_LAST * kC];
-            float need[2], size[2], keep[2] = {last, last};
-            most_rows(buf.most, lane, need);
-            most_rows(buf.s_most, lane, size);
-            bool off = false;
+            float need[2], left[2], keep[2] = {last, last};
+            most_rows<true>(buf.most, lane, need);
+            most_rows(buf.s_most, lane, left);
+            bool off = false, lost = false;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                need[q] = fmaxf(need[q], size[q] * last * kUnderState);
+                left[q] *= last * kUnderState;
+                need[q] = max_or_nan(need[q], left[q], 0.f);
                 off |= Domain::off(need[q]);
             }
-            if (__any_sync(0xFFFFFFFFu, off)) {
+            Cut cut;
+            if (__builtin_expect(__any_sync(0xFFFFFFFFu, off), 0)) {
+                lost = __any_sync(0xFFFFFFFFu, !is_finite(need[0]) || !is_finite(need[1]));
+                if (lost) {
+                    cut.find(B, buf.most, me, lane);
+                    cut.fill(B, lane, 0.f);
+                    cut.fill(X, lane, 0.f);
+                    cut.fill(Y, lane, kNan);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        if (!is_finite(need[q])) keep[q] = kNan;
+                    row_max<2>(B, m);
+                    team_sync(team);  // `most` has been read
+                    share_rows(buf.most[me], m, lane);
+                    team_sync(team);
+                    most_rows(buf.most, lane, need);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        if (is_finite(left[q])) need[q] = fmaxf(need[q], left[q]);
+                }
                 float f[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -297,6 +352,7 @@ __device__ __forceinline__ void walk(const DeltaArgs &a, const Saved &saved, Rin
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) t[x][j] = X[x][j] * dom.up[j >> 1];
+                if (lost) cut.fill(t, lane, kNan);
                 store_image<kC>(saved.u + (hc * 2 * v16 + col) * kC, t, lane, (long long)v16 * kC / 2, mine);
             }
             // U as operands: l U for P, w U for the state

@@ -84,6 +84,11 @@ enum { W_UK, W_UQ, W_Q2, W_K2, W_BETA, W_EG, W_EW, W_RK, W_LK, W_RQ, W_FQ, kWork
 // 3.4 waves.  Five CTAs at 96 registers take as long here and 35 us instead of 32
 // for 32 chunks x 32 heads, which are two waves either way; whole rows of blocks a
 // warp, 1 to 4 of them, took 48.6.
+//
+// A token's key, gate or beta may be no finite number.  Its row of K, its sum of
+// gates and its beta are then zeros in all that M and P are made of, so that rows
+// of tokens before it stay as they are; e^G of its key is no number, by which the
+// walk finds where outputs and state are lost.
 template <typename T, int KD, bool VEC>
 __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 1 : 4) delta_prep_kernel(DeltaArgs a, Prepared w, int nchunks) {
     constexpr int NT = terms16<T>(), TILE = kC * KD, BT = terms(!std::is_same<T, __nv_bfloat16>::value);
@@ -129,16 +134,16 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 1 : 4) delta_pr
         for (int x = 0; x < PART; ++x) {
             mk[x] = mq[x] = sq[x] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                mk[x] = fmaxf(mk[x], fabsf(kr[x].get(i)));
-                mq[x] = fmaxf(mq[x], fabsf(qr[x].get(i)));
+            for (int i = 0; i < 8; i += 2) {
+                mk[x] = max_or_nan(mk[x], fabsf(kr[x].get(i)), fabsf(kr[x].get(i + 1)));
+                mq[x] = fmaxf(fmaxf(mq[x], fabsf(qr[x].get(i))), fabsf(qr[x].get(i + 1)));
             }
         }
 #pragma unroll
         for (int o = 1; o < UNITS; o *= 2)
 #pragma unroll
             for (int x = 0; x < PART; ++x) {
-                mk[x] = fmaxf(mk[x], __shfl_xor_sync(0xFFFFFFFFu, mk[x], o));
+                mk[x] = max_or_nan(mk[x], __shfl_xor_sync(0xFFFFFFFFu, mk[x], o), 0.f);
                 mq[x] = fmaxf(mq[x], __shfl_xor_sync(0xFFFFFFFFu, mq[x], o));
             }
 #pragma unroll
@@ -160,6 +165,11 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 1 : 4) delta_pr
             if (NT == 2) {
                 *reinterpret_cast<uint4 *>(kq + TILE + at) = make_uint4(kl.r[0], kl.r[1], kl.r[2], kl.r[3]);
                 *reinterpret_cast<uint4 *>(kq + (NT + 1) * TILE + at) = make_uint4(ql.r[0], ql.r[1], ql.r[2], ql.r[3]);
+            }
+            if (!is_finite(mk[x])) {
+                *reinterpret_cast<uint4 *>(kq + at) = make_uint4(0, 0, 0, 0);
+                if (NT == 2) *reinterpret_cast<uint4 *>(kq + TILE + at) = make_uint4(0, 0, 0, 0);
+                uk = kNan;
             }
             if (u == 0) {
                 work[W_UK * kC + r] = uk;
@@ -207,15 +217,16 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 1 : 4) delta_pr
             const double up = __shfl_up_sync(0xFFFFFFFFu, run, o);
             if (lane >= o) run += up;
         }
-        s[0] = run - s[1];
+        const double before = __shfl_up_sync(0xFFFFFFFFu, run, 1);
+        if (lane > 0) s[0] += before;  // not run - s[1], which need be no number where s[0] is one
         s[1] = run;
         const double last = __shfl_sync(0xFFFFFFFFu, run, 31);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int r = 2 * lane + j;
-            const float hi = (float)s[j];
+            const float hi = finite_or_zero((float)s[j]);
             gh[r] = hi;
-            gl[r] = (float)(s[j] - hi);
+            gl[r] = finite_or_zero((float)(s[j] - hi));
             work[W_BETA * kC + r] = be[j];
             work[W_EG * kC + r] = __expf((float)s[j]);
             work[W_EW * kC + r] = __expf((float)(last - s[j]));
@@ -294,14 +305,14 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 1 : 4) delta_pr
         // |k| = sqrt(k2) uk; the eps of the norms belongs to the unscaled sum
         const float nk = a.qk_norm ? rsqrtf(fmaf(k2 * uk, uk, kDeltaEps)) : 1.f;
         const float nq = a.qk_norm ? rsqrtf(fmaf(q2 * uq, uq, kDeltaEps)) : 1.f;
-        const float fk = uk * nk, lk = k2 * rk * fk, lq = q2 * rq * uq * nq;
+        const float fk = uk * nk, lk = finite_or_zero(k2 * rk * fk), lq = q2 * rq * uq * nq;
         const float eg = at(W_EG), ew = at(W_EW);
         at(W_RK) = rk;
         at(W_LK) = lk;
         at(W_RQ) = rq;
         at(W_FQ) = lq * a.scale;
-        vec16[F_LB * kC + tid] = lk * be;
-        vec16[F_EK * kC + tid] = eg * fk;
+        vec16[F_LB * kC + tid] = finite_or_zero(lk * be);
+        vec16[F_EK * kC + tid] = fmaf(0.f, be, eg * fk);  // no number where beta is none
         vec16[F_EQ * kC + tid] = eg * rq;
         vec16[F_WB * kC + tid] = be * ew * fk;
         vec16[F_FQ * kC + tid] = lq * a.scale;

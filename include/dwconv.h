@@ -412,10 +412,13 @@ dwconv_status dwconv_block_norm_bwd(long long rows_outer, int rows_inner, int C,
  *   S_t = e^g_t S_(t-1) + beta_t k_t (v_t - e^g_t S_(t-1)^T k_t)^T,  o_t = scale S_t^T q_t.
  * q, k [B][T][Hk][K], v [B][T][Hv][V], g (log decay) and beta [B][T][Hv]; Hv a
  * multiple of Hk (value head h reads key head h / (Hv / Hk)); 1 <= K <= 256.
- * g of minus infinity, or so low that e^g is zero, resets the state.  Sequences
- * that run in chunks want sums of positive g over 64 tokens below 10 and
- * beta |k|^2 below 2^15 (fp16 operands); a rule that does not grow has g <= 0
- * and beta |k|^2 <= 2.
+ * g of minus infinity, or so low that e^g is zero, resets the state.  The rule
+ * is meant not to grow: g <= 0 and beta |k|^2 <= 2, as with qk_norm and beta in
+ * [0, 2].  Where it grows by more than 2^15 within 64 tokens, a sequence that
+ * runs in chunks leaves the range of its fp16 operands and gives NaN.  A NaN or
+ * an infinity in an input reaches the outputs of its token and of later ones
+ * (one in v only those of its column, one in q only its token's), never earlier
+ * ones; gradients may be lost before it too.
  * g and beta are of gate_dtype: dtype or DWCONV_FP32.  With qk_norm, q and k
  * are divided by sqrt(sum x^2 + 1e-6) first.  strides: batch, token and head
  * strides of q, k, v, g, beta (15 values; NULL: dense).  state float

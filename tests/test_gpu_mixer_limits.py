@@ -76,3 +76,49 @@ def test_gates_that_reset_a_state(T, dtype, gates, value):
     for name, a, r in zip((*delta_bwd.NAMES, "dstate"), got, want):
         ref.assert_close_in_norm(a, r, name, delta_bwd.REL[dtype])
     assert not got[3][g < -1e4].any()  # nothing depends on how far below
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("what", ["v", "k", "q", "g", "beta"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("t", [0, 5, 17, 63, 64, 100])
+def test_values_that_are_no_numbers_leave_earlier_tokens_alone(dtype, what, bad, t):
+    """What one token's NaN or infinity does to the outputs is the rule's own: nothing before it, and of v's columns
+    only its own; the state and every later output of what it reaches is not finite."""
+    args, state = delta.inputs(dtype, 1, 150, 1, 2, 64, 48, seed=13, norm=False)
+    names = ("q", "k", "v", "g", "beta")
+    want, clean = dw.dwconv_delta_fwd(*args, qk_norm=False, state=state, return_state=True)
+    dirty = [a.clone() for a in args]
+    hit = dirty[names.index(what)]
+    if hit.dim() == 4:
+        hit[0, t, 0, 3] = bad
+    else:
+        hit[0, t, 0] = bad
+    o, after = dw.dwconv_delta_fwd(*dirty, qk_norm=False, state=state, return_state=True)
+    # A column's power of two is chosen from what a whole chunk adds to it: other splits of the same values.
+    ref.assert_close_in_norm(o[:, :t], ref.wide(want[:, :t]), "earlier tokens", delta.REL[dtype])
+    reached = torch.zeros_like(want, dtype=torch.bool)
+    if what == "v":
+        reached[0, t:, 0, 3] = True
+    elif what == "q":
+        reached[0, t] = True  # both value heads read the query
+    elif what == "k":
+        reached[0, t:] = True
+    else:
+        reached[0, t:, 0] = True
+    if what in "vq":
+        apart = ~reached
+        if what == "v":
+            apart[0, :, 0, 3] = False
+        assert torch.equal(o[apart], want[apart])
+    elif what != "k":
+        assert torch.equal(o[:, :, 1], want[:, :, 1])
+    assert not torch.isfinite(o[reached]).any()
+    lost = torch.zeros_like(after, dtype=torch.bool)
+    if what == "v":
+        lost[0, 0, :, 3] = True
+    elif what == "k":
+        lost[:] = True
+    elif what != "q":
+        lost[0, 0] = True
+    assert torch.equal(after[~lost], clean[~lost]) and not torch.isfinite(after[lost]).any()
