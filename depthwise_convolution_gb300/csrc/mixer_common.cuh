@@ -75,7 +75,8 @@ cudaError_t launch_after(void (*kern)(A...), dim3 grid, dim3 block, size_t smem,
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    if (e != cudaSuccess) (void)cudaGetLastError();  // told here, not to who asks next
+    return e;
 }
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 

@@ -10,8 +10,9 @@
 // kernels, and takes 143.
 //
 // What a function accepts is exactly what the Python function that calls it
-// accepts; anything else raises here without words, and the Python function then
-// finds out what to say.
+// accepts.  For anything else it returns NotImplemented before it has done
+// anything, and the Python function finds out what to say.  What fails later is
+// raised as it is, once: the call is not made again.
 #include <Python.h>
 
 #include <ATen/ATen.h>
@@ -23,6 +24,8 @@
 
 #include <cmath>
 #include <cstdint>
+#include <stdexcept>
+#include <string>
 
 #include "dwconv.h"
 
@@ -44,12 +47,24 @@ Tensor like(const Tensor &t) { return t.defined() ? at::empty(t.sizes(), t.optio
 Tensor bytes(size_t n, const Tensor &ref) {
     return n ? at::empty({(int64_t)n}, ref.options().dtype(at::kByte)) : Tensor();
 }
+// A call that the library refused or that failed.
+struct Failed : std::runtime_error {
+    dwconv_status status;
+    const char *where;
+    Failed(dwconv_status st, const char *where_)
+        : std::runtime_error(std::string(where_) + ": " + dwconv_status_string(st)), status(st), where(where_) {}
+};
 void check(dwconv_status st, const char *where) {
-    TORCH_CHECK(st == DWCONV_OK, where, ": ", dwconv_status_string(st));
+    if (st != DWCONV_OK) throw Failed(st, where);
 }
 
-// Every requirement on an argument; the message is the Python function's.
-void need(bool ok) { TORCH_CHECK(ok, "unsupported arguments"); }
+// Every requirement on an argument; the words are the Python function's.
+struct Refused : std::runtime_error {
+    Refused() : std::runtime_error("unsupported arguments") {}
+};
+void need(bool ok) {
+    if (!ok) throw Refused();
+}
 dwconv_dtype code_of(at::ScalarType t) {
     need(t == at::kFloat || t == at::kHalf || t == at::kBFloat16);
     return t == at::kFloat ? DWCONV_FP32 : t == at::kHalf ? DWCONV_FP16 : DWCONV_BF16;
@@ -136,6 +151,7 @@ struct CausalNode : torch::autograd::Function<CausalNode> {
 
 Tensor causal_conv(const Tensor &x, const Tensor &w, const Optional &bias, const Optional &state, const Optional &n,
                    int64_t act) {
+    need(x.is_cuda());
     const c10::DeviceGuard guard(x.device());
     if (wants_grad({x, w, given(bias), given(state)})) return CausalNode::apply(x, w, bias, state, n, act);
     return Causal(x, w, given(bias), given(state), given(n), act)
@@ -144,6 +160,7 @@ Tensor causal_conv(const Tensor &x, const Tensor &w, const Optional &bias, const
 
 variable_list causal_fwd(const Tensor &x, const Tensor &w, const Optional &bias, const Optional &state,
                          const Optional &n, int64_t act, bool with_state) {
+    need(x.is_cuda());
     const c10::DeviceGuard guard(x.device());
     return Causal(x, w, given(bias), given(state), given(n), act)
         .forward(x, w, given(bias), given(state), given(n), with_state);
@@ -151,6 +168,7 @@ variable_list causal_fwd(const Tensor &x, const Tensor &w, const Optional &bias,
 
 Tensor causal_step(const Tensor &x, const Tensor &w, const Tensor &state, const Optional &bias, const Optional &slots,
                    int64_t act) {
+    need(x.is_cuda());
     const c10::DeviceGuard guard(x.device());
     need(x.dim() == 2 && w.dim() == 2 && state.dim() == 3);
     const int B = count(x.size(0)), C = count(x.size(1)), W = count(w.size(0)), N = count(state.size(0));
@@ -270,6 +288,7 @@ struct NormNode : torch::autograd::Function<NormNode> {
 
 variable_list block_norm(const Tensor &y, const Optional &residual, const Optional &gate, const Optional &w_post,
                          const Optional &scale, const Optional &w_pre, int64_t kind, int64_t act, double eps) {
+    need(y.is_cuda());
     const c10::DeviceGuard guard(y.device());
     const variable_list in{y, given(residual), given(gate), given(w_post), given(scale), given(w_pre)};
     if (wants_grad({in[0], in[1], in[2], in[3], in[4], in[5]}))
@@ -279,6 +298,7 @@ variable_list block_norm(const Tensor &y, const Optional &residual, const Option
 
 variable_list block_norm_fwd(const Tensor &y, const Optional &residual, const Optional &gate, const Optional &w_post,
                              const Optional &scale, const Optional &w_pre, int64_t kind, int64_t act, double eps) {
+    need(y.is_cuda());
     const c10::DeviceGuard guard(y.device());
     const variable_list in{y, given(residual), given(gate), given(w_post), given(scale), given(w_pre)};
     return Norm(in, kind, act, eps).forward(in);
@@ -373,6 +393,7 @@ struct DeltaNode : torch::autograd::Function<DeltaNode> {
 variable_list gated_delta_rule(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor &g, const Tensor &beta,
                                const Optional &state, const Optional &n, std::optional<double> scale, bool qk_norm,
                                bool with_state) {
+    need(q.is_cuda());
     const c10::DeviceGuard guard(q.device());
     if (wants_grad({q, k, v, g, beta, given(state)}))
         return DeltaNode::apply(q, k, v, g, beta, state, n, scale, qk_norm, with_state);
@@ -382,6 +403,7 @@ variable_list gated_delta_rule(const Tensor &q, const Tensor &k, const Tensor &v
 
 Tensor delta_step(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor &g, const Tensor &beta,
                   const Tensor &state, const Optional &slots, std::optional<double> scale, bool qk_norm) {
+    need(q.is_cuda());
     const c10::DeviceGuard guard(q.device());
     const Delta s({q, k, v, g, beta}, 1, scale, qk_norm);
     const Tensor at = given(slots);
@@ -437,11 +459,26 @@ template <typename F> auto unlocked(F &&f) {
     return f();
 }
 
+// Raises the package's own error.
+PyObject *raise(const Failed &e) {
+    PyObject *lib = PyImport_ImportModule("depthwise_convolution_gb300._lib");
+    PyObject *none = lib ? PyObject_CallMethod(lib, "check", "is", (int)e.status, e.where) : nullptr;
+    Py_XDECREF(none);
+    Py_XDECREF(lib);
+    return nullptr;
+}
+
 #define DWCONV_METHOD(name, count, call)                                              \
     PyObject *py_##name(PyObject *, PyObject *const *args, Py_ssize_t given) {        \
         HANDLE_TH_ERRORS                                                              \
-        const Args p(args, given, count);                                             \
-        return call;                                                                  \
+        try {                                                                         \
+            const Args p(args, given, count);                                         \
+            return call;                                                              \
+        } catch (const Refused &) {                                                   \
+            Py_RETURN_NOTIMPLEMENTED;                                                 \
+        } catch (const Failed &e) {                                                   \
+            return raise(e);                                                          \
+        }                                                                             \
         END_HANDLE_TH_ERRORS                                                          \
     }
 

@@ -16,11 +16,11 @@ def causal_conv(x, w, bias=None, act="silu", state=None, lengths=None):
     bias [C] float32, state [B,W-1,C], lengths [B] int32 (see dwconv_causal_fwd)."""
     if isinstance(w, torch.Tensor) and not w.is_contiguous():
         w = w.contiguous()
-    try:
-        return ops._native("causal_conv")(x, w, bias, state, lengths, ops._act(act))
-    except RuntimeError:
+    out = ops._native("causal_conv")(x, w, bias, state, lengths, ops._act(act))
+    if out is NotImplemented:
         ops._causal_sequence(x, w, bias, act, state, lengths)  # says what is wrong with them
-        raise
+        raise ValueError("unsupported arguments")
+    return out
 
 
 def gated_delta_rule(q, k, v, g, beta, scale=None, qk_norm=False, state=None, lengths=None, return_state=False):
@@ -28,12 +28,10 @@ def gated_delta_rule(q, k, v, g, beta, scale=None, qk_norm=False, state=None, le
     state [B,Hv,K,V] float32 (see dwconv_delta_fwd); K <= 128 for gradients.  Returns o,
     with return_state (o, last state).  Keeps the forward pass's chunk tiles for the
     backward pass where a gradient is wanted."""
-    try:
-        out = ops._native("gated_delta_rule")(q, k, v, g, beta, state, lengths, scale, bool(qk_norm),
-                                              bool(return_state))
-    except RuntimeError:
+    out = ops._native("gated_delta_rule")(q, k, v, g, beta, state, lengths, scale, bool(qk_norm), bool(return_state))
+    if out is NotImplemented:
         ops._delta_checks(q, k, v, g, beta, 2, state, (lengths, "lengths"))
-        raise
+        raise ValueError("unsupported arguments")
     return out if return_state else out[0]
 
 
@@ -42,12 +40,11 @@ def block_norm(y, residual=None, gate=None, w_post=None, scale=None, w_pre=None,
     """Differentiable norms around a block: (h, n) with h = residual + scale * post(y) *
     act(gate) and n = pre(h), or n None without w_pre (see dwconv_block_norm_fwd)."""
     codes = ops._choice(ops.NORMS, kind, "norm"), ops._choice(ops.GATES, gate_act, "gate activation")
-    try:
-        out = ops._native("block_norm")(y, residual, gate, w_post, scale, w_pre, *codes, eps)
-    except RuntimeError:
+    out = ops._native("block_norm")(y, residual, gate, w_post, scale, w_pre, *codes, eps)
+    if out is NotImplemented:
         ops._norm_checks(((y, "y"), (residual, "residual"), (gate, "gate")),
                          ((w_post, "w_post"), (scale, "scale"), (w_pre, "w_pre")), kind, gate_act)
-        raise
+        raise ValueError("unsupported arguments")
     return (out[0], out[1]) if w_pre is not None else (out[0], None)
 
 

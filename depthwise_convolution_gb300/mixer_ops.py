@@ -35,7 +35,7 @@ def _module():
 
 def _native(name):
     """A function of libdwconv_torch.so.  It takes what the function here that calls it takes, with new outputs on the
-    current stream, and raises RuntimeError for anything else, about which that function then has the words."""
+    current stream, and returns NotImplemented for anything else, about which that function then has the words."""
     op = _NATIVE.get(name)
     if op is None:
         op = _NATIVE[name] = getattr(_module(), name)
@@ -197,11 +197,9 @@ def dwconv_causal_fwd(x, w, bias=None, act="silu", state=None, lengths=None, ret
     zeros), lengths [B] int32 (right padding beyond) or None.  Returns y [B,T,C], with
     return_state (y, state_out): the window that the live tokens leave."""
     if out is None and state_out is None and stream is None:
-        try:
-            done = _native("causal_fwd")(x, w, bias, state, lengths, _act(act), bool(return_state))
+        done = _native("causal_fwd")(x, w, bias, state, lengths, _act(act), bool(return_state))
+        if done is not NotImplemented:
             return done if return_state else done[0]
-        except RuntimeError:
-            pass
     dt, dev, (B, T, C, W), code, xs = _causal_sequence(x, w, bias, act, state, lengths)
     with _region(dev, stream):
         out, op = _new(out, "out", (B, T, C), dev, x)
@@ -246,10 +244,9 @@ def dwconv_causal_step(x, w, state, bias=None, act="silu", slots=None, out=None,
     slots [B] int32 names each row's window (None: its own row; outside [0,N): the row
     is idle and gives zeros).  Returns y [B,C]."""
     if out is None and stream is None:
-        try:
-            return _native("causal_step")(x, w, state, bias, slots, _act(act))
-        except RuntimeError:
-            pass
+        done = _native("causal_step")(x, w, state, bias, slots, _act(act))
+        if done is not NotImplemented:
+            return done
     try:
         key = ("causal step", act, _meta(x), _meta(w), _meta(state), _meta(bias), _meta(slots))
         known = _SEEN.get(key)
@@ -337,12 +334,10 @@ def dwconv_block_norm_fwd(y, residual=None, gate=None, w_post=None, scale=None, 
     "rms" or "layer", gate_act "silu", "sigmoid" or "none".  Returns (h, n), n None
     without w_pre."""
     if stream is None:
-        try:
-            done = _native("block_norm_fwd")(y, residual, gate, w_post, scale, w_pre, _choice(NORMS, kind, "norm"),
-                                             _choice(GATES, gate_act, "gate activation"), eps)
+        done = _native("block_norm_fwd")(y, residual, gate, w_post, scale, w_pre, _choice(NORMS, kind, "norm"),
+                                         _choice(GATES, gate_act, "gate activation"), eps)
+        if done is not NotImplemented:
             return (done[0], done[1] if w_pre is not None else None)
-        except RuntimeError:
-            pass
     dt, dev, outer, inner, C, strides, norm, act = _norm_checks(
         ((y, "y"), (residual, "residual"), (gate, "gate")), ((w_post, "w_post"), (scale, "scale"), (w_pre, "w_pre")),
         kind, gate_act)
@@ -491,10 +486,9 @@ def dwconv_delta_step(q, k, v, g, beta, state, scale=None, qk_norm=False, slots=
     state [N,Hv,K,V] float32, updated in place; slots as in dwconv_causal_step.  Returns
     o [B,Hv,V]."""
     if out is None and stream is None:
-        try:
-            return _native("delta_step")(q, k, v, g, beta, state, slots, scale, bool(qk_norm))
-        except RuntimeError:
-            pass
+        done = _native("delta_step")(q, k, v, g, beta, state, slots, scale, bool(qk_norm))
+        if done is not NotImplemented:
+            return done
     (B,), (Hk, Hv, K, V), dt, dev, gdt, strides = _delta_checks(q, k, v, g, beta, 1, state, (slots, "slots"))
     with _region(dev, stream):
         out, op = _new(out, "out", (B, Hv, V), dev, q)
