@@ -43,6 +43,10 @@ float *float_target(const Tensor &t) { return static_cast<float *>(target(t)); }
 const int *lengths_of(const Tensor &t) { return static_cast<const int *>(address(t)); }
 Tensor given(const Optional &t) { return t ? *t : Tensor(); }
 dwconv_stream stream_of(const Tensor &t) { return c10::cuda::getCurrentCUDAStream(t.get_device()).stream(); }
+// The caller's tensor is written in place: autograd has to see that.
+void written(const Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 Tensor like(const Tensor &t) { return t.defined() ? at::empty(t.sizes(), t.options()) : Tensor(); }
 Tensor bytes(size_t n, const Tensor &ref) {
     return n ? at::empty({(int64_t)n}, ref.options().dtype(at::kByte)) : Tensor();
@@ -183,6 +187,7 @@ Tensor causal_step(const Tensor &x, const Tensor &w, const Tensor &state, const 
     check(dwconv_causal_step(B, N, C, W, dt, address(x), x.stride(0), address(w), floats(b), (dwconv_activation)act,
                              target(state), lengths_of(at), target(y), stream_of(x)),
           "dwconv_causal_step");
+    written(state);
     return y;
 }
 
@@ -415,6 +420,7 @@ Tensor delta_step(const Tensor &q, const Tensor &k, const Tensor &v, const Tenso
                             address(v), address(g), address(beta), s.strides.data(), s.scale, s.qk_norm,
                             float_target(state), lengths_of(at), target(o), stream_of(q)),
           "dwconv_delta_step");
+    written(state);
     return o;
 }
 

@@ -135,12 +135,20 @@ def _longs(*values):
     return (ctypes.c_longlong * len(values))(*values)
 
 
+def _written(t):
+    """The caller's tensor is written in place: autograd has to see that."""
+    if not t.is_inference():
+        torch.autograd.graph.increment_version(t)
+
+
 def _new(out, name, shape, dev, ref, dtype=None):
     """(tensor, address) of an output: the caller's, or a new one."""
     if out is None:
         out = torch.empty(shape, dtype=dtype or ref.dtype, device=ref.device)
         return out, out.data_ptr()
-    return out, _dense(out, name, shape, dev, dtype or ref.dtype)
+    p = _dense(out, name, shape, dev, dtype or ref.dtype)
+    _written(out)
+    return out, p
 
 
 def _scratch(workspace, need, ref):
@@ -265,6 +273,7 @@ def dwconv_causal_step(x, w, state, bias=None, act="silu", slots=None, out=None,
         _lib.check(_ll().dwconv_causal_step(B, N, C, W, dt, x.data_ptr(), xs, w.data_ptr(), _address(bias), code,
                                             state.data_ptr(), _address(slots), op, _current(dev)),
                    "dwconv_causal_step")
+    _written(state)
     return out
 
 
@@ -496,4 +505,5 @@ def dwconv_delta_step(q, k, v, g, beta, state, scale=None, qk_norm=False, slots=
             B, state.shape[0], Hk, Hv, K, V, dt, gdt, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
             beta.data_ptr(), _longs(*strides), K ** -0.5 if scale is None else scale, int(qk_norm), state.data_ptr(),
             _address(slots), op, _current(dev)), "dwconv_delta_step")
+    _written(state)
     return out

@@ -33,3 +33,31 @@ def test_the_window_has_its_gradient_with_and_without_a_bias(with_bias, with_len
     # test_gpu_causal_conv.py's bound for gradients, 4e-6 of the summed magnitudes: W taps of at most 1.1 |dy| |w|
     size = 4 * 1.1 * dy.abs().max().item() * w.abs().max().item() * torch.ones_like(rs)
     ref.assert_near(window.grad, rs, "dstate", "fp32", 4e-6, size)
+
+
+def test_states_written_in_place_raise_their_version():
+    g = torch.Generator().manual_seed(6)
+    scale = torch.randn((), generator=g).cuda().requires_grad_()
+    x, w, window = (torch.randn(*s, generator=g).cuda() for s in ((2, 16), (4, 16), (2, 3, 16)))
+    q, v, gate = torch.randn(2, 1, 16, generator=g).cuda(), torch.randn(2, 1, 8, generator=g).cuda(), \
+        -torch.rand(2, 1, generator=g).cuda()
+    state = torch.randn(2, 1, 16, 8, generator=g).cuda()
+    out = torch.empty(2, 16, device="cuda")
+    seq = [t[:, None] for t in (q, q, v, gate, gate.neg())]
+    calls = [(window, lambda: dw.dwconv_causal_step(x, w, window)),
+             (window, lambda: dw.dwconv_causal_step(x, w, window, out=out)),
+             (out, lambda: dw.dwconv_causal_step(x, w, window, out=out)),
+             (state, lambda: dw.dwconv_delta_step(q, q, v, gate, gate.neg(), state)),
+             (state, lambda: dw.dwconv_delta_step(q, q, v, gate, gate.neg(), state, stream=torch.cuda.current_stream())),
+             (state, lambda: dw.dwconv_delta_fwd(*seq, state=state, state_out=state)),
+             (window, lambda: dw.dwconv_causal_fwd(x[:, None], w, state_out=window))]
+    for t, call in calls:
+        kept = (t * scale).sum()
+        before = t._version
+        call()
+        assert t._version > before
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            kept.backward()
+    with torch.inference_mode():  # tensors without a version
+        dw.dwconv_causal_step(x, w, torch.zeros(2, 3, 16, device="cuda"))
+        dw.dwconv_delta_step(q, q, v, gate, gate.neg(), torch.zeros(2, 1, 16, 8, device="cuda"), out=torch.empty_like(v))
