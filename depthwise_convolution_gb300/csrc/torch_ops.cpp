@@ -89,7 +89,12 @@ void need_dense(const Tensor &t, at::IntArrayRef shape, const Tensor &ref, at::S
     need(t.is_contiguous());
 }
 
+// Whether a backward pass may follow.  Tangents of forward mode, which goes on
+// without gradients, are refused: they would be lost.
 bool wants_grad(std::initializer_list<Tensor> in) {
+    for (const Tensor &t : in)
+        TORCH_CHECK_NOT_IMPLEMENTED(!t.defined() || !t._fw_grad(/*level=*/0).defined(),
+                                    "the token mixer's operations have no forward-mode derivatives");
     if (!at::GradMode::is_enabled()) return false;
     for (const Tensor &t : in)
         if (t.defined() && t.requires_grad()) return true;

@@ -35,6 +35,34 @@ def test_the_window_has_its_gradient_with_and_without_a_bias(with_bias, with_len
     ref.assert_near(window.grad, rs, "dstate", "fp32", 4e-6, size)
 
 
+def operations():
+    """(name, function of its differentiable inputs, those inputs): each of the three operations."""
+    g = torch.Generator().manual_seed(5)
+    x, w = torch.randn(2, 30, 16, generator=g).cuda(), torch.randn(4, 16, generator=g).cuda()
+    y, one = torch.randn(6, 32, generator=g).cuda(), torch.ones(32).cuda()
+    q, k, v = (torch.randn(1, 30, 1, 16, generator=g).cuda() for _ in range(3))
+    gate, beta = -torch.rand(1, 30, 1, generator=g).cuda(), torch.rand(1, 30, 1, generator=g).cuda()
+    return [("causal_conv", lambda *a: dw.causal_conv(*a), [x, w]),
+            ("block_norm", lambda *a: dw.block_norm(a[0], w_post=a[1])[0], [y, one]),
+            ("gated_delta_rule", lambda *a: dw.gated_delta_rule(*a, qk_norm=True), [q, k, v, gate, beta])]
+
+
+@pytest.mark.parametrize("which", range(3))
+def test_forward_mode_is_refused(which):
+    import torch.autograd.forward_ad as fwd
+    name, f, args = operations()[which]
+    plain = f(*args)
+    for requires in (False, True):
+        with fwd.dual_level():
+            dual = [fwd.make_dual(a.clone().requires_grad_(requires), torch.ones_like(a)) if i == 0 else a
+                    for i, a in enumerate(args)]
+            with pytest.raises(RuntimeError, match="forward"):
+                f(*dual)
+            with torch.no_grad(), pytest.raises(RuntimeError, match="forward"):
+                f(*dual)
+    assert torch.equal(f(*args), plain)
+
+
 def test_states_written_in_place_raise_their_version():
     g = torch.Generator().manual_seed(6)
     scale = torch.randn((), generator=g).cuda().requires_grad_()
