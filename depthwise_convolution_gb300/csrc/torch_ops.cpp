@@ -316,6 +316,8 @@ variable_list block_norm_fwd(const Tensor &y, const Optional &residual, const Op
 
 // ---- gated delta rule
 
+constexpr int kMostGradK = 128;
+
 // Inputs of a call, B x (T x) heads x values, the gates B x (T x) value heads.
 struct Delta {
     dwconv_dtype dt, gate_dt;
@@ -370,6 +372,7 @@ struct DeltaNode : torch::autograd::Function<DeltaNode> {
                                  std::optional<double> scale, bool qk_norm, bool with_state) {
         const variable_list in{q, k, v, g, beta};
         const Delta s(in, 2, scale, qk_norm);
+        need(s.K <= kMostGradK);  // what the backward pass takes
         const Tensor saved = bytes(dwconv_delta_saved_size(s.B, s.T, s.Hk, s.Hv, s.K, s.V, s.dt), q);
         ctx->save_for_backward({q, k, v, g, beta, given(state), given(n), saved});
         ctx->saved_data["scale"] = scale;

@@ -30,8 +30,8 @@ def gated_delta_rule(q, k, v, g, beta, scale=None, qk_norm=False, state=None, le
     backward pass where a gradient is wanted."""
     out = ops._native("gated_delta_rule")(q, k, v, g, beta, state, lengths, scale, bool(qk_norm), bool(return_state))
     if out is NotImplemented:
-        ops._delta_checks(q, k, v, g, beta, 2, state, (lengths, "lengths"))
-        raise ValueError("unsupported arguments")
+        (_, _), (_, _, K, _), *_ = ops._delta_checks(q, k, v, g, beta, 2, state, (lengths, "lengths"))
+        raise ValueError(f"gradients take keys of at most 128 values, got {K}" if K > 128 else "unsupported arguments")
     return out if return_state else out[0]
 
 

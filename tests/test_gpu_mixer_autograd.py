@@ -89,3 +89,13 @@ def test_states_written_in_place_raise_their_version():
     with torch.inference_mode():  # tensors without a version
         dw.dwconv_causal_step(x, w, torch.zeros(2, 3, 16, device="cuda"))
         dw.dwconv_delta_step(q, q, v, gate, gate.neg(), torch.zeros(2, 1, 16, 8, device="cuda"), out=torch.empty_like(v))
+
+
+def test_keys_too_wide_for_gradients_are_refused_at_once():
+    q, v = torch.randn(1, 20, 1, 200, device="cuda"), torch.randn(1, 20, 1, 16, device="cuda", requires_grad=True)
+    gate = torch.zeros(1, 20, 1, device="cuda")
+    with pytest.raises(ValueError, match="128"):
+        dw.gated_delta_rule(q, q, v, gate, gate)
+    with torch.no_grad():
+        assert dw.gated_delta_rule(q, q, v, gate, gate).shape == v.shape
+    assert dw.gated_delta_rule(q, q, v.detach(), gate, gate).shape == v.shape
