@@ -100,6 +100,23 @@ bool wants_grad(std::initializer_list<Tensor> in) {
         if (t.defined() && t.requires_grad()) return true;
     return false;
 }
+// The gradients come out of kernels that have no backward pass of their own: under
+// create_graph they would look like constants.  This node says that they are none.
+struct Once : torch::autograd::Function<Once> {
+    static Tensor forward(AutogradContext *, const Tensor &grad, const Tensor &) { return grad; }
+    static variable_list backward(AutogradContext *, variable_list) {
+        TORCH_CHECK_NOT_IMPLEMENTED(false, "the token mixer's operations cannot be differentiated twice");
+    }
+};
+// A backward pass's gradients; `in` and `up`: what they depend on.
+variable_list once(variable_list grads, const variable_list &in, const variable_list &up) {
+    if (!at::GradMode::is_enabled()) return grads;
+    for (Tensor &g : grads)
+        for (const variable_list *from : {&in, &up})  // on the way to each of them: what is not asked for is not run
+            for (const Tensor &t : *from)
+                if (g.defined() && t.defined() && t.requires_grad()) g = Once::apply(g, t);
+    return grads;
+}
 // The last dimension dense, as the kernels want it.
 Tensor dense_rows(const Tensor &t) { return t.stride(-1) == 1 ? t : t.contiguous(); }
 
@@ -154,7 +171,7 @@ struct CausalNode : torch::autograd::Function<CausalNode> {
                                 lengths_of(in[4]), target(dx), float_target(dw), float_target(db), target(ds),
                                 target(work), size, stream_of(x)),
               "dwconv_causal_bwd");
-        return {dx, dw.to(w.scalar_type()), db, ds, Tensor(), Tensor()};
+        return once({dx, dw.to(w.scalar_type()), db, ds, Tensor(), Tensor()}, in, up);
     }
 };
 
@@ -292,7 +309,7 @@ struct NormNode : torch::autograd::Function<NormNode> {
                                     float_target(grads[3]), float_target(grads[4]), float_target(grads[5]),
                                     target(work), size, stream_of(in[0])),
               "dwconv_block_norm_bwd");
-        return grads;
+        return once(std::move(grads), in, up);
     }
 };
 
@@ -399,7 +416,7 @@ struct DeltaNode : torch::autograd::Function<DeltaNode> {
                                target(grads[1]), target(grads[2]), target(grads[3]), target(grads[4]),
                                float_target(grads[5]), address(saved), target(work), size, stream_of(q)),
               "dwconv_delta_bwd");
-        return grads;
+        return once(std::move(grads), in, up);
     }
 };
 

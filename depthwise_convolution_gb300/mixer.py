@@ -2,7 +2,8 @@
 
 ``causal_conv``, ``gated_delta_rule`` and ``block_norm`` check their arguments and call native autograd nodes (which
 only marshal arguments and save inputs, every pass runs in the library's kernels); ``GatedDeltaMixer`` puts them
-together as a layer.
+together as a layer.  They are differentiable once and in reverse: forward mode and the derivative of a gradient raise
+NotImplementedError.
 """
 from __future__ import annotations
 

@@ -63,6 +63,24 @@ def test_forward_mode_is_refused(which):
     assert torch.equal(f(*args), plain)
 
 
+@pytest.mark.parametrize("which", range(3))
+def test_second_derivatives_are_refused(which):
+    name, f, args = operations()[which]
+    leaves = [a.requires_grad_() for a in args]
+    out = f(*leaves)
+    for up in (torch.ones_like(out), torch.ones_like(out).requires_grad_()):
+        first = torch.autograd.grad(out, leaves, up, create_graph=True)
+        plain = torch.autograd.grad(out, leaves, up.detach(), retain_graph=True)
+        assert all(torch.equal(a, b) for a, b in zip(first, plain))
+        for d in first:  # a penalty on a gradient, beside a term that has a history of its own
+            with pytest.raises(RuntimeError, match="twice"):
+                torch.autograd.grad(d.square().sum() + leaves[0].square().sum(), leaves, retain_graph=True,
+                                    allow_unused=True)
+            for leaf in leaves:  # whichever is asked for
+                with pytest.raises(RuntimeError, match="twice"):
+                    torch.autograd.grad(d.square().sum() + leaf.square().sum(), leaf, retain_graph=True)
+
+
 def test_states_written_in_place_raise_their_version():
     g = torch.Generator().manual_seed(6)
     scale = torch.randn((), generator=g).cuda().requires_grad_()
