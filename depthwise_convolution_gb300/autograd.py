@@ -5,7 +5,8 @@ Tensors are channels-last and dense: x [N, H, W, C], w [FH, FW, C], bias [C]
 ``dwconv_fwd``; the backward pass calls ``dwconv_bwd_data`` for dx,
 ``dwconv_bwd_filter`` for dw (float32, cast to w's dtype) and
 ``dwconv_bwd_bias`` for db.  This module only marshals arguments; every pass
-runs in the library's kernels.  int8 data is forward only.
+runs in the library's kernels.  int8 data is forward only.  The derivative of a
+gradient (create_graph) raises NotImplementedError.
 """
 from __future__ import annotations
 
@@ -14,6 +15,18 @@ import math
 import torch
 
 from . import ops
+
+
+class _Once(torch.autograd.Function):
+    """Passes a gradient on, whose kernels have no backward pass: under create_graph it would look like a constant."""
+
+    @staticmethod
+    def forward(ctx, grad, *depends_on):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, grad):
+        raise NotImplementedError("depthwise_conv2d cannot be differentiated twice")
 
 
 class DepthwiseConv2dFunction(torch.autograd.Function):
@@ -41,6 +54,8 @@ class DepthwiseConv2dFunction(torch.autograd.Function):
                                        half_accumulate=ctx.half_accumulate).to(w.dtype)
         if ctx.bias_dtype is not None and ctx.needs_input_grad[2]:
             db = ops.dwconv_bwd_bias(dy).to(ctx.bias_dtype)
+        if torch.is_grad_enabled():
+            dx, dw, db = (None if d is None else _Once.apply(d, *on) for d, on in ((dx, (w, dy)), (dw, (x, dy)), (db, (dy,))))
         return dx, dw, db, None, None, None, None
 
 
