@@ -67,6 +67,12 @@ bool good_strides(const long long *s, int n) {
     return true;
 }
 
+// Whether two buffers of `bytes` bytes share one.
+bool overlap(const void *p, const void *q, size_t bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && (a < b ? b - a : a - b) < bytes;
+}
+
 struct Sized {
     const void *p;
     size_t size;
@@ -169,6 +175,8 @@ dwconv_status dwconv_causal_fwd(int B, int T, int C, int W, dwconv_dtype dtype, 
     const bool some = B > 0 && T > 0;
     if (some && (!x || !w || !y)) return DWCONV_ERR_INVALID_ARG;
     const size_t es = float_size(dtype);
+    // a row's last segment writes its window while the first may still read the one before
+    if (overlap(state, state_out, es * B * (W - 1) * C)) return DWCONV_ERR_INVALID_ARG;
     if (!all_aligned({{x, es}, {w, es}, {bias, 4}, {state, es}, {lengths, 4}, {y, es}, {state_out, es}}))
         return DWCONV_ERR_MISALIGNED;
     if (B == 0 || (T == 0 && (!state_out || W == 1))) return DWCONV_OK;
@@ -306,6 +314,7 @@ dwconv_status dwconv_delta_fwd(int B, int T, int Hk, int Hv, int K, int V, dwcon
     if (st != DWCONV_OK) return st;
     if (!good_strides(strides, 15)) return DWCONV_ERR_INVALID_ARG;
     if (B > 0 && T > 0 && (!q || !k || !v || !g || !beta || !out)) return DWCONV_ERR_INVALID_ARG;
+    if (state != state_out && overlap(state, state_out, sizeof(float) * B * Hv * K * V)) return DWCONV_ERR_INVALID_ARG;
     if (saved && K > chunk::kMaxK) return DWCONV_ERR_UNSUPPORTED;
     const size_t need = saved ? 0 : dwconv_delta_fwd_workspace_size(B, T, Hk, Hv, K, V, dtype);
     if (need > 0 && (!workspace || workspace_bytes < need)) return DWCONV_ERR_INVALID_ARG;

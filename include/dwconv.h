@@ -340,7 +340,8 @@ dwconv_status dwconv_bwd_filter_ha(int N, int H, int W, int C, int FH, int FW, i
  * NULL (zeros); lengths [B] (live tokens per row, the rest is right padding
  * that is never read) or NULL (all T).  y [B][T][C] dense, zero in the
  * padding; state_out [B][W-1][C] (nullable): the last W-1 live tokens of the
- * sequence continued from the state.
+ * sequence continued from the state, in a buffer apart from it (overlapping:
+ * DWCONV_ERR_INVALID_ARG).
  */
 dwconv_status dwconv_causal_fwd(int B, int T, int C, int W, dwconv_dtype dtype, const void *x, long long x_batch,
                                 long long x_row, const void *w, const float *bias, dwconv_activation act,
@@ -423,8 +424,9 @@ dwconv_status dwconv_block_norm_bwd(long long rows_outer, int rows_inner, int C,
  * are divided by sqrt(sum x^2 + 1e-6) first.  strides: batch, token and head
  * strides of q, k, v, g, beta (15 values; NULL: dense).  state float
  * [B][Hv][K][V] or NULL (zeros); lengths as above; out [B][T][Hv][V] dense,
- * zero in the padding; state_out float (nullable; may be `state` itself): the
- * state after the last live token.  saved (nullable, K <= 128,
+ * zero in the padding; state_out float (nullable; may be `state` itself, but
+ * not overlap it otherwise: DWCONV_ERR_INVALID_ARG): the state after the last
+ * live token.  saved (nullable, K <= 128,
  * dwconv_delta_saved_size bytes, 16-byte aligned): what dwconv_delta_bwd can
  * take over instead of repeating the forward pass; the workspace is then not
  * used.  Sequences of more than 10 tokens with K <= 128 run in chunks of 64 on
