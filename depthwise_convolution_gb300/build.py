@@ -6,7 +6,8 @@ runtime linked statically).  ``-Xptxas -v`` output is kept in
 ``_build/ptxas.log`` (registers, spills, shared memory per kernel).
 ``csrc/torch_ops.cpp`` (the token mixer's calls on PyTorch tensors, with their
 autograd nodes) compiles beside them with g++ and becomes ``libdwconv_torch.so``,
-a Python extension module linked to the first.
+a Python extension module linked to the first; without PyTorch the C library is
+built alone.
 """
 from __future__ import annotations
 
@@ -47,18 +48,28 @@ def _deps():
                                                                    os.path.abspath(__file__)]
 
 
+def _torch():
+    try:
+        import torch
+    except ImportError:
+        return None
+    return torch
+
+
 def needs_build() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(OPS):
+    made = [LIB] if _torch() is None else [LIB, OPS]
+    if not all(os.path.exists(p) for p in made):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(OPS))
+    t = min(os.path.getmtime(p) for p in made)
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
-def _compile_ops() -> tuple:
+def _compile_ops() -> tuple | None:
     import sysconfig
 
-    import torch
-
+    torch = _torch()
+    if torch is None:
+        return None
     at = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     obj = os.path.join(BUILD, "torch_ops.o")
@@ -88,11 +99,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(os.cpu_count() or 8, len(srcs) + 1)) as ex:
         ops = ex.submit(_compile_ops)
         results = list(ex.map(_compile, srcs))
-    log = []
+    log, made = [], ops.result()
     for src, obj, rc, out in results:
         log.append(f"==== {os.path.basename(src)}\n{out}")
         if rc != 0:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{out}")
+    if made is not None and made[2] != 0:
+        raise RuntimeError(f"g++ failed on {os.path.basename(made[0])}:\n{made[3]}")
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         f.write("\n".join(log))
     tmp = LIB + f".tmp{os.getpid()}"
@@ -101,15 +114,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}{r.stderr}")
     os.replace(tmp, LIB)
-    src, parts, rc, out = ops.result()
-    if rc != 0:
-        raise RuntimeError(f"g++ failed on {os.path.basename(src)}:\n{out}")
-    tmp = OPS + f".tmp{os.getpid()}"
-    r = subprocess.run(["g++", "-shared", "-o", tmp, parts[0], "-L", PKG, "-ldwconv", *parts[1:], "-Wl,-rpath,$ORIGIN"],
-                       capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ link failed:\n{r.stdout}{r.stderr}")
-    os.replace(tmp, OPS)
+    if made is not None:
+        obj, *libs = made[1]
+        tmp = OPS + f".tmp{os.getpid()}"
+        r = subprocess.run(["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-ldwconv", *libs, "-Wl,-rpath,$ORIGIN"],
+                           capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ link failed:\n{r.stdout}{r.stderr}")
+        os.replace(tmp, OPS)
     if verbose:
         print("\n".join(log))
     return LIB
