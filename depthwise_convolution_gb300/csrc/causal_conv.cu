@@ -466,21 +466,30 @@ cudaError_t launch_causal_fwd(int B, int T, int C, int W, dwconv_dtype dt, const
 // holds one slice per kRows segments of a row): the length whose waves of blocks
 // take the fewest steps, with the W-1 tokens that a segment re-reads and the
 // checked ones at its ends counted as 12 more, on 152 SMs of 4 blocks (8 of
-// single channels).  4 x 4096 x 4096 bf16: 114 tokens, 109 us; 16 take 173, 48
-// 122, 128 104, 512 126.  1 x 777 x 2304 fp16: 8 tokens, 20 us; 64 take 28.
+// single channels).  4 x 4096 x 4096 bf16: 114 tokens, 98 us (fp32 132); 16 take
+// 162 (166), 64 102 (145), 128 94 (134), 147 92 (142), 256 100 (127), 512 118
+// (156): the rule is within 7 % of the best.  2 x 4097 x 2304 bf16: 65 tokens, 35;
+// 32 take 40, 128 45.  1 x 777 x 2304 fp16: 8 tokens, 10.6; 32 take 14, 64 19.
 int causal_bwd_segment(long long B, long long T, long long C) {
+    constexpr long long kLeast = 8;  // only the first segment reaches back before the sequence
     const bool whole = C % 4 == 0;
     const long long slots = 152 * (whole ? 4 : 8), columns = B * ((C + (whole ? 127 : 31)) / (whole ? 128 : 32));
-    long long best = 0, seg = 8;
-    for (long long groups = 1; groups == 1 || groups * kRows * 8 < T + kRows * 8; ++groups) {
-        // at least 8: only the first segment reaches back before the sequence
-        const long long s = std::max((T + groups * kRows - 1) / (groups * kRows), 8LL);
-        const long long cost = (columns * groups + slots - 1) / slots * (s + 12);
-        if (groups == 1 || cost < best) {
+    // Groups of kRows segments a row, at most: none of the shortest length is empty, and no more than eight waves
+    // of segments up to 1024 tokens need.
+    const long long full = (T + kRows * kLeast - 1) / (kRows * kLeast);
+    const long long enough = std::max((T + kRows * 1024 - 1) / (kRows * 1024), 8 * slots / columns + 1);
+    const long long most = std::max(std::min(full, enough), 1LL);
+    // Of the numbers of groups that take the same waves the largest has the shortest segments: one try a wave.
+    long long best = 0, seg = kLeast;
+    for (long long groups = 0, waves = (columns + slots - 1) / slots; groups < most; ++waves) {
+        if (waves * slots < (groups + 1) * columns) waves = ((groups + 1) * columns + slots - 1) / slots;
+        groups = std::min(waves * slots / columns, most);
+        const long long s = std::max((T + groups * kRows - 1) / (groups * kRows), kLeast);
+        const long long cost = waves * (s + 12);
+        if (best == 0 || cost < best) {
             best = cost;
             seg = s;
         }
-        if (s <= 1024 && columns * groups > 8 * slots) break;
     }
     return (int)seg;
 }
