@@ -1,5 +1,7 @@
 """The token mixer at the edges of what it accepts: widths, gates and values where a kernel's form changes or a sum could
 leave the finite numbers.  Tolerances are those of the operator's own test file, which derives them."""
+import threading
+
 import pytest
 import torch
 
@@ -122,3 +124,65 @@ def test_values_that_are_no_numbers_leave_earlier_tokens_alone(dtype, what, bad,
     elif what != "q":
         lost[0, 0] = True
     assert torch.equal(after[~lost], clean[~lost]) and not torch.isfinite(after[lost]).any()
+
+
+@pytest.mark.parametrize("dtype,shape,kind", [("bf16", (400, 8200), "rms"), ("fp32", (330, 8192), "layer"),
+                                              ("bf16", (320, 16384), "rms"), ("fp16", (310, 10001), "layer")])
+def test_norm_gradients_of_the_widest_rows_on_many_rows(dtype, shape, kind):
+    norms.test_gradients(dtype, shape, kind, "sigmoid", "rgpsn", "both")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_write_strengths_up_to_two(dtype):
+    """beta between 0 and 2 turns a key's direction over instead of overwriting it; the rule still does not grow."""
+    args, state = delta.inputs(dtype, 2, 200, 1, 2, 64, 48, seed=17)
+    args[4] = args[4] * 2
+    args[4][:, 70:90] = 2
+    do = torch.randn(args[2].shape, generator=torch.Generator().manual_seed(18)).to(args[2].dtype).cuda()
+    o, after = dw.dwconv_delta_fwd(*args, qk_norm=True, state=state, return_state=True)
+    got = dw.dwconv_delta_bwd(do, *args, qk_norm=True, state=state, need_dstate=True)
+    leaves = [ref.leaf(a) for a in (*args, state)]
+    ro, rs = ref.delta(*leaves[:5], None, True, leaves[5], None)
+    want = torch.autograd.grad((ro * ref.wide(do)).sum(), leaves)
+    ref.assert_close_in_norm(o, ro, "o", delta.REL[dtype])
+    ref.assert_close_in_norm(after, rs, "state", 2e-5)
+    for name, a, r in zip((*delta_bwd.NAMES, "dstate"), got, want):
+        ref.assert_close_in_norm(a, r, name, delta_bwd.REL[dtype])
+
+
+def test_calls_from_two_host_threads():
+    """Each thread with a stream and shapes of its own gets what a single one gets."""
+    def work(seed, C, T):
+        g = torch.Generator().manual_seed(seed)
+        x, y = (torch.randn(2, T, C, generator=g).cuda().requires_grad_() for _ in range(2))
+        w, one = torch.randn(4, C, generator=g).cuda(), torch.ones(C).cuda()
+        gates = -torch.rand(2, T, 1, generator=g).cuda()
+
+        def run():
+            heads = dw.causal_conv(x, w).unflatten(-1, (1, C))
+            o = dw.gated_delta_rule(heads, heads, heads, gates, gates.neg(), qk_norm=True)
+            h, _ = dw.block_norm(o.flatten(-2), y, w_post=one)
+            return [h.detach(), *torch.autograd.grad(h.square().sum(), (x, y))]
+        return run
+
+    runs = [work(1, 64, 200), work(2, 48, 130)]
+    want = [run() for run in runs]
+    torch.cuda.synchronize()
+    off, failed = [], []
+
+    def thread(run, expected):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30):
+                    got = run()
+                    torch.cuda.current_stream().synchronize()
+                    off.extend(i for i, (a, b) in enumerate(zip(got, expected)) if not torch.equal(a, b))
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=thread, args=a) for a in zip(runs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed and not off
