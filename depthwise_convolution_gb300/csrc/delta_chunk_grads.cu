@@ -411,10 +411,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int t = t0 + r + j;
-                // nothing comes through a decay of zero; the sum above has the roundings of terms that cancel
+                // nothing comes through a decay of zero or out of an empty past; the sum above has the roundings
+                // of terms that cancel
                 const float *gh = vec + V_GH * kC + r + j, *gl = vec + V_GL * kC + r + j;
                 const float g = r + j ? (gh[0] - gh[-1]) + (gl[0] - gl[-1]) : gh[0] + gl[0];
-                if (__expf(g) == 0.f) dg[j] = 0.f;
+                if (__expf(g) == 0.f || (t == 0 && !a.state)) dg[j] = 0.f;
                 if (t < end) {
                     put_gate(d.dg, t, h, t < n ? dg[j] : 0.f);
                     put_gate(d.dbeta, t, h, t < n ? diag[r + j] : 0.f);

@@ -186,3 +186,19 @@ def test_calls_from_two_host_threads():
     for t in threads:
         t.join()
     assert not failed and not off
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T", [1, 2, 70])
+def test_an_empty_past_does_not_depend_on_the_first_decay(T, dtype):
+    """Without a state the first token's decay acts on zeros: its gradient is zero, whatever follows."""
+    args, _ = delta.inputs(dtype, 2, T, 1, 2, 64, 48, seed=19)
+    g = torch.Generator().manual_seed(20)
+    do, last = torch.randn(args[2].shape, generator=g).to(args[2].dtype).cuda(), torch.randn(2, 2, 64, 48, generator=g).cuda()
+    got = dw.dwconv_delta_bwd(do, *args, qk_norm=True, dstate_out=last)
+    assert not got[3][:, 0].any() and (T == 1 or got[3][:, 1:].any())
+    leaves = [ref.leaf(a) for a in args]
+    ro, rs = ref.delta(*leaves, None, True, None, None)
+    want = torch.autograd.grad((ro * ref.wide(do)).sum() + (rs * ref.wide(last)).sum(), leaves)
+    for name, a, r in zip(delta_bwd.NAMES, got, want):
+        ref.assert_close_in_norm(a, r, name, delta_bwd.REL[dtype])
