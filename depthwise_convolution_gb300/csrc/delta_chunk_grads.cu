@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 // of terms that cancel
                 const float *gh = vec + V_GH * kC + r + j, *gl = vec + V_GL * kC + r + j;
                 const float g = r + j ? (gh[0] - gh[-1]) + (gl[0] - gl[-1]) : gh[0] + gl[0];
-                if (__expf(g) == 0.f || (t == 0 && !a.state)) dg[j] = 0.f;
+                if (__expf(g) == 0.f || (t == 0 && !a.state)) dg[j] *= 0.f;  // a NaN stays one
                 if (t < end) {
                     put_gate(d.dg, t, h, t < n ? dg[j] : 0.f);
                     put_gate(d.dbeta, t, h, t < n ? diag[r + j] : 0.f);

@@ -202,3 +202,26 @@ def test_an_empty_past_does_not_depend_on_the_first_decay(T, dtype):
     want = torch.autograd.grad((ro * ref.wide(do)).sum() + (rs * ref.wide(last)).sum(), leaves)
     for name, a, r in zip(delta_bwd.NAMES, got, want):
         ref.assert_close_in_norm(a, r, name, delta_bwd.REL[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("what", ["v", "k", "q", "g", "beta", "do", "last"])
+@pytest.mark.parametrize("t", [0, 5, 63, 100])
+def test_gradients_that_are_lost_are_not_made_up(dtype, what, t):
+    """Wherever the definition's gradient is no number because an input is none, the kernels' is none."""
+    args, state = delta.inputs(dtype, 1, 150, 1, 2, 64, 48, seed=21, norm=False)
+    g = torch.Generator().manual_seed(22)
+    do, last = torch.randn(args[2].shape, generator=g).to(args[2].dtype).cuda(), torch.randn(1, 2, 64, 48, generator=g).cuda()
+    hit = dict(zip(("q", "k", "v", "g", "beta", "do", "last"), (*args, do, last)))[what]
+    hit[(0, t, 0, 3)[:hit.dim()] if what != "last" else (0, 0, 7, 3)] = float("nan")
+    for past in (state, None):
+        leaves = [ref.leaf(a) for a in args] + ([] if past is None else [ref.leaf(past)])
+        ro, rs = ref.delta(*leaves[:5], None, False, None if past is None else leaves[5], None)
+        want = torch.autograd.grad((ro * ref.wide(do)).sum() + (rs * ref.wide(last)).sum(), leaves)
+        saved = torch.empty(dw.dwconv_delta_saved_size(1, 150, 1, 2, 64, 48, args[0].dtype), dtype=torch.uint8, device="cuda")
+        dw.dwconv_delta_fwd(*args, state=past, saved=saved)
+        for s in (saved, None):
+            got = dw.dwconv_delta_bwd(do, *args, state=past, dstate_out=last, need_dstate=past is not None, saved=s)
+            for name, a, r in zip((*delta_bwd.NAMES, "dstate"), got, want):
+                made_up = torch.isfinite(ref.wide(a)) & ~torch.isfinite(r)
+                assert not made_up.any(), f"{name}: {int(made_up.sum())} of {r.numel()}, first {made_up.nonzero()[0].tolist()}"
