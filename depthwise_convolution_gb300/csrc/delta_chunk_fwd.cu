@@ -299,10 +299,10 @@ __device__ __forceinline__ void walk(const DeltaArgs &a, const Saved &saved, Rin
                 need[q] = max_or_nan(need[q], left[q], 0.f);
                 off |= Domain::off(need[q]);
             }
-            Cut cut;
             if (__builtin_expect(__any_sync(0xFFFFFFFFu, off), 0)) {
                 lost = __any_sync(0xFFFFFFFFu, !is_finite(need[0]) || !is_finite(need[1]));
                 if (lost) {
+                    Cut cut;
                     cut.find(B, buf.most, me, lane);
                     cut.fill(B, lane, 0.f);
                     cut.fill(X, lane, 0.f);
@@ -352,7 +352,11 @@ __device__ __forceinline__ void walk(const DeltaArgs &a, const Saved &saved, Rin
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) t[x][j] = X[x][j] * dom.up[j >> 1];
-                if (lost) cut.fill(t, lane, kNan);
+                if (lost)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) t[x][j] = fmaf(0.f, Y[x][j], t[x][j]);  // lost with its output
                 store_image<kC>(saved.u + (hc * 2 * v16 + col) * kC, t, lane, (long long)v16 * kC / 2, mine);
             }
             // U as operands: l U for P, w U for the state
