@@ -117,16 +117,17 @@ template <typename F> __device__ __forceinline__ void with_act(int act, F &&f) {
     else f(std::integral_constant<int, DWCONV_GATE_NONE>{});
 }
 
-// A thread's columns of a row of any tensor, and of the weight vectors; the row's
-// end where a vector of its lies beyond.
+// A thread's columns of a row of any tensor, and of the weight vectors; `ends`: the
+// row's end where a vector of its lies beyond.
 template <int VEC, int NV> struct Cols {
     int c[NV];
     bool in[NV];
-    __device__ __forceinline__ Cols(const NormArgs &a, int g) {
+    __device__ __forceinline__ Cols(const NormArgs &a, int g, bool ends = false) {
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
-            c[q] = min((q * a.G + g) * VEC, a.C);
+            c[q] = (q * a.G + g) * VEC;
             in[q] = c[q] < a.C;
+            if (ends) c[q] = min(c[q], a.C);
         }
     }
     // One vector's worth of a weight vector (ones where it is absent); all CTAs of
@@ -194,12 +195,14 @@ template <int VEC, int NV, bool HOLD> struct Weight {
 
 // The same out of shared memory, where the backward pass, which has no
 // registers left for them, keeps its weight vectors: ones where a vector is
-// absent, and behind the row one vector of zeros for all columns beyond it.
-template <int VEC, int NV> struct SharedWeight {
+// absent, zeros beyond the row.  Beside a ring all columns beyond share one vector
+// of zeros behind the row; elsewhere, where there is room, each has its own (the
+// widest rows' form spills, and the shared one's addresses cost it 4 %).
+template <int VEC, int NV, bool RING> struct SharedWeight {
     const float *w;
-    static __host__ __device__ int size(int C) { return C + VEC; }
+    static __host__ __device__ int size(int C, int G) { return RING ? C + VEC : G * NV * VEC; }
     __device__ __forceinline__ SharedWeight(const NormArgs &a, const float *from, float *to) : w(to) {
-        for (int c = threadIdx.x; c < size(a.C); c += blockDim.x) to[c] = c < a.C ? (from ? from[c] : 1.f) : 0.f;
+        for (int c = threadIdx.x; c < size(a.C, a.G); c += blockDim.x) to[c] = c < a.C ? (from ? from[c] : 1.f) : 0.f;
     }
     __device__ __forceinline__ Pack<float, VEC> at(const Cols<VEC, NV> &cols, int q) const {
         if constexpr (VEC == 1) {
@@ -532,12 +535,12 @@ __global__ void __launch_bounds__(MAXT, MAXT == 128 ? (NV * VEC <= 8 ? 4 : 3) : 
     __shared__ RowRing ring;
     extern __shared__ __align__(128) unsigned char smem[];  // weights, then the ring; afterwards [rows per CTA][C] column sums
     float *shared_cols = reinterpret_cast<float *>(smem), *weights = shared_cols;
-    const int width = SharedWeight<VEC, NV>::size(a.C);
+    const int width = SharedWeight<VEC, NV, RING>::size(a.C, a.G);
     unsigned char *stages = smem + 3 * width * sizeof(float);
     after_previous();
     Group group(red, a.G);
-    const Cols<VEC, NV> cols(a, threadIdx.x % a.G);
-    const SharedWeight<VEC, NV> post(a, a.w_post, weights), scale(a, a.scale, weights + width),
+    const Cols<VEC, NV> cols(a, threadIdx.x % a.G, RING);
+    const SharedWeight<VEC, NV, RING> post(a, a.w_post, weights), scale(a, a.scale, weights + width),
         pre(a, a.w_pre, weights + 2 * width);
     __syncthreads();
     float s_post[NV][VEC], s_scale[NV][VEC], s_pre[NV][VEC];
@@ -773,7 +776,7 @@ cudaError_t fwd_run(const NormArgs &a, int threads, cudaStream_t st) {
 template <typename T, int VEC, int NV, int MAXT, bool RING>
 cudaError_t bwd_run(const NormArgs &a, int threads, float *dwp, float *dsc, float *dwr, cudaStream_t st) {
     const int per = threads / a.G;
-    const size_t smem = std::max(3 * sizeof(float) * SharedWeight<VEC, NV>::size(a.C) + (RING ? a.stages * round_bytes<T>(a, per) : 0),
+    const size_t smem = std::max(3 * sizeof(float) * SharedWeight<VEC, NV, RING>::size(a.C, a.G) + (RING ? a.stages * round_bytes<T>(a, per) : 0),
                                  per > 1 ? (size_t)per * a.C * sizeof(float) : 0);
     auto kern = block_norm_bwd_kernel<T, VEC, NV, MAXT, RING>;
     long long grid = 0;
