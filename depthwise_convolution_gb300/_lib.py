@@ -69,7 +69,8 @@ class DwconvError(RuntimeError):
 
 
 def lib_path() -> str:
-    """The in-tree library, or the build named by DWCONV_LIB (for A/B timing)."""
+    """The in-tree library, or the build named by DWCONV_LIB (for A/B timing; the extension module of
+    :func:`load_torch_ops` stays with the in-tree one)."""
     return os.environ.get("DWCONV_LIB") or _build.LIB
 
 

@@ -414,7 +414,7 @@ template <typename T, int VEC, int NV, bool RING> struct Input {
 // Forward.  A thread holds 16 values of a row and the weights for them.  What
 // bounds it is instructions (about 30 a value at 4096 columns, half of them for
 // the row: sums, addresses, barriers): 16384 rows of 4096 in bf16 with residual,
-// scale and both norms take 98 us, 5.45 TB/s; with three weight vectors and the
+// scale and both norms take 97 us, 5.55 TB/s; with three weight vectors and the
 // inputs in registers 109, with 32 values a thread and the weights read from L1
 // for each row 118, and with divisions and loops in the sums 132.  Three CTAs of
 // 256 threads an SM instead of two spill at 80 registers: 127.
@@ -523,12 +523,15 @@ __device__ __forceinline__ void norm_back(float (&u)[NV][VEC], const float (&hat
 
 // Backward: CTAs stay like the forward's, with their column sums in registers,
 // the weights in shared memory and the inputs read from the ring where they are
-// used.  8192 rows of 2048 in bf16 with all parts and a sigmoid gate take 105 us
-// (2.55 TB/s): four sums of a row follow one another, on 12 warps an SM, with some
+// used.  8192 rows of 2048 in bf16 with all parts and a sigmoid gate take 103 us
+// (2.6 TB/s): four sums of a row follow one another, on 12 warps an SM, with some
 // 95 instructions a value, half of them arithmetic (the gate is evaluated twice:
 // no registers are left to keep it).  Choices per value took 129; a fourth
 // CTA an SM spills at 128 registers (133), except with eight values a thread
-// (fp32, 16384 x 768: 81 us instead of 97).
+// (fp32, 16384 x 768: 81 us instead of 97).  From 256 threads a row on 128
+// registers are the limit of 512 threads: 16-bit rows of more than 2048 columns
+// spill a little (8192 x 4096 bf16 292 us, fp32 196; 4096 x 7040 218), the widest
+// rows' form a lot (4096 x 8192 bf16 515, fp32 658; 2048 x 16384 522, 668).
 template <typename T, int VEC, int NV, int MAXT, bool RING>
 __global__ void __launch_bounds__(MAXT, MAXT == 128 ? (NV * VEC <= 8 ? 4 : 3) : 1) block_norm_bwd_kernel(NormArgs a) {
     __shared__ float red[2][NV_MAX][32];

@@ -6,9 +6,10 @@
 // read as zero.  W multiply-adds per element against four bytes moved: the floor
 // is memory, so a thread owns a few adjacent channels and walks down the tokens
 // with the window in registers, and each x is read once apart from the W-1 tokens
-// that neighbouring segments share.  4 x 4096 x 4096 bf16, W = 4, SiLU: forward 51
-// us (5.3 TB/s), backward 99 us (4.1 TB/s; 27 instructions an element, five of
-// them the two special functions of a sigmoid, at 0.5 a cycle and scheduler).
+// that neighbouring segments share.  4 x 4096 x 4096 bf16, W = 4, SiLU: forward 52
+// us (5.1 TB/s), backward 98 us (4.1 TB/s: 122 registers leave 16 warps an SM, which
+// issue 0.5 instructions a cycle and scheduler, 27 an element, five of them the two
+// special functions of a sigmoid).  fp32: 89 us (6.0 TB/s) and 132 us (6.1 TB/s).
 #include <algorithm>
 
 #include "mixer_common.cuh"

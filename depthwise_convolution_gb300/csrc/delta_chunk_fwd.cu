@@ -18,8 +18,8 @@
 // instructions one after the other, some six cycles apart with two warps a
 // scheduler (issue 0.34 a cycle, shared memory 62 % of its rate); heads x V / 16
 // column groups seldom fill the 608 sub-partitions, so a group is worth four
-// warps.  32 heads x 4097 tokens, K = V = 128, bf16: 163 us, against 232 with two
-// warps a group and 248 with one.  With a copy of the code per block assignment,
+// warps.  32 heads x 4097 tokens, K = V = 128, bf16: 164 us, against 232 with two
+// warps a group and 248 with one (2 to 3 us are what inputs that are no numbers cost).  With a copy of the code per block assignment,
 // waiting for instructions was the largest stall; now the blocks' bounds are
 // tested in unrolled loops (rolled ones: 10 us more).  Partial sums of S K^T
 // shared instead of the state's operands took as long with one meeting more.

@@ -10,7 +10,7 @@
 //
 // which is the output of the new state without a second pass over it.  A
 // single token moves 8 K V bytes of state per head and little else: the floor
-// is memory.  250 rows of 16 heads, K = V = 128: 89 us, 5.9 TB/s of the 524 MB;
+// is memory.  240 live rows of 250, 16 heads, K = V = 128: 88 us, 5.7 TB/s of 506 MB;
 // one row 4.7 us, a chain of latencies.
 #include "delta.cuh"
 

@@ -69,7 +69,8 @@ class GatedDeltaMixer(torch.nn.Module):
       q, k, v = SiLU(conv(n W)),  o = delta(q, k, v, g, beta),
       h' = h + scale * (norm(o) SiLU(gate)) W_out,  n' = norm(h').
     ``prefill`` and ``step`` do the same against a :class:`MixerCache`.  The projections
-    are plain matrix products; everything else runs in the library's kernels.
+    are plain matrix products, decay and write strength plain PyTorch operations on one
+    value a head and token; everything else runs in the library's kernels.
     """
 
     def __init__(self, width, key_heads, value_heads, key_width=128, value_width=128, taps=4, dtype=torch.bfloat16,
