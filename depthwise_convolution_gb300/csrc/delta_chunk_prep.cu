@@ -85,9 +85,9 @@ enum { W_UK, W_UQ, W_Q2, W_K2, W_BETA, W_EG, W_EW, W_RK, W_LK, W_RQ, W_FQ, kWork
 // for 32 chunks x 32 heads, which are two waves either way; whole rows of blocks a
 // warp, 1 to 4 of them, took 48.6.
 //
-// A token's key, gate or beta may be no finite number.  Its row of K, its sum of
-// gates and its beta are then zeros in all that M and P are made of, so that rows
-// of tokens before it stay as they are; e^G of its key is no number, by which the
+// A token's key, gate or beta may be no finite number.  Its row of K and its beta
+// are then zeros, its sum of gates a low number in all that M and P are made of, so
+// that rows of tokens before it stay as they are; e^G of its key is no number, by which the
 // walk finds where outputs and state are lost.
 template <typename T, int KD, bool VEC>
 __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 1 : 4) delta_prep_kernel(DeltaArgs a, Prepared w, int nchunks) {
@@ -224,9 +224,11 @@ __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 1 : 4) delta_pr
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int r = 2 * lane + j;
-            const float hi = finite_or_zero((float)s[j]);
+            // a sum that is none stands below all others: decays from there are 0 or, among such, 1
+            const bool sum = is_finite((float)s[j]);
+            const float hi = sum ? (float)s[j] : 256 * kDeltaReset;
             gh[r] = hi;
-            gl[r] = finite_or_zero((float)(s[j] - hi));
+            gl[r] = sum ? (float)(s[j] - hi) : 0.f;
             work[W_BETA * kC + r] = be[j];
             work[W_EG * kC + r] = __expf((float)s[j]);
             work[W_EW * kC + r] = __expf((float)(last - s[j]));

@@ -204,6 +204,24 @@ def test_an_empty_past_does_not_depend_on_the_first_decay(T, dtype):
         ref.assert_close_in_norm(a, r, name, delta_bwd.REL[dtype])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("what", ["v", "k", "g", "beta"])
+def test_what_is_no_number_behind_strong_decays(dtype, what, bad):
+    """The same behind decays that leave nothing, where the inverse of one overflows."""
+    args, state = delta.inputs(dtype, 1, 60, 1, 2, 64, 48, seed=23, norm=False)
+    args[3][:, 2::7] = -90
+    args[3][:, 5::11] = float("-inf")
+    want = dw.dwconv_delta_fwd(*args, state=state)
+    hit = args[("q", "k", "v", "g", "beta").index(what)]
+    for t in (41, 24, 9):
+        dirty = hit.clone()
+        dirty[(0, t, 0, 3)[:hit.dim()]] = bad
+        o, after = dw.dwconv_delta_fwd(*(dirty if a is hit else a for a in args), state=state, return_state=True)
+        ref.assert_close_in_norm(o[:, :t], ref.wide(want[:, :t]), "earlier tokens", delta.REL[dtype])
+        assert not torch.isfinite(o[0, t:, 0, 3]).any() and not torch.isfinite(after[0, 0, :, 3]).any()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("what", ["v", "k", "q", "g", "beta", "do", "last"])
 @pytest.mark.parametrize("t", [0, 5, 63, 100])
