@@ -19,9 +19,10 @@
 // scheduler (issue 0.34 a cycle, shared memory 62 % of its rate); heads x V / 16
 // column groups seldom fill the 608 sub-partitions, so a group is worth four
 // warps.  32 heads x 4097 tokens, K = V = 128, bf16: 164 us, against 232 with two
-// warps a group and 248 with one (2 to 3 us are what inputs that are no numbers cost).  With a copy of the code per block assignment,
-// waiting for instructions was the largest stall; now the blocks' bounds are
-// tested in unrolled loops (rolled ones: 10 us more).  Partial sums of S K^T
+// warps a group and 248 with one (162 without the branch for inputs that are no
+// numbers).  With a copy of the code per block assignment, waiting for
+// instructions was the largest stall; now the blocks' bounds are tested in
+// unrolled loops (rolled ones: 10 us more).  Partial sums of S K^T
 // shared instead of the state's operands took as long with one meeting more.
 // Scaling the state's rows for each product and back took 175 us, scales per
 // block of tokens 174.

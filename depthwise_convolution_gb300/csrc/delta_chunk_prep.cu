@@ -87,8 +87,8 @@ enum { W_UK, W_UQ, W_Q2, W_K2, W_BETA, W_EG, W_EW, W_RK, W_LK, W_RQ, W_FQ, kWork
 //
 // A token's key, gate or beta may be no finite number.  Its row of K and its beta
 // are then zeros, its sum of gates a low number in all that M and P are made of, so
-// that rows of tokens before it stay as they are; e^G of its key is no number, by which the
-// walk finds where outputs and state are lost.
+// that rows of tokens before it stay as they are; e^G of its key is no number, by
+// which the walk finds where outputs and state are lost.
 template <typename T, int KD, bool VEC>
 __global__ void __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 1 : 4) delta_prep_kernel(DeltaArgs a, Prepared w, int nchunks) {
     constexpr int NT = terms16<T>(), TILE = kC * KD, BT = terms(!std::is_same<T, __nv_bfloat16>::value);
